@@ -67,15 +67,11 @@ size_t carve_bytes(int64_t rows, int64_t cols) {
 }
 
 // X quantized (x.codes), or bf16 rows (x_bf16) that the product quantizes.
-// early: the kernel queued just before this product is the same call's and
-// does not write the weights.  A kernel starts only when every CTA of the one
-// before has passed its own pdl_wait, so all kernels before that one are done,
-// and weights that one of them wrote are there.
-cudaError_t product(bool early, const mxfp4_tensor& x, const uint16_t* x_bf16, int64_t ldx, const mxfp4_tensor& w, const mxfp4_tensor* up, int act, void* y,
-                    int y_dtype, int64_t ldy, const mxfp4_tensor* qy, cudaStream_t s) {
+cudaError_t product(const mxfp4_tensor& x, const uint16_t* x_bf16, int64_t ldx, const mxfp4_tensor& w,
+                    const mxfp4_tensor* up, int act, void* y, int y_dtype, int64_t ldy, const mxfp4_tensor* qy,
+                    cudaStream_t s) {
   Mx4Gemm g{};
   g.x = {x.codes, x.scales};
-  g.early = early;
   g.x_bf16 = x_bf16;
   g.ldx = ldx;
   g.w = {w.codes, w.scales};
@@ -156,7 +152,7 @@ nvfp4_status mxfp4_gemm_quantized(const mxfp4_tensor* qa, const mxfp4_tensor* qb
   NV_CHECK(y != nullptr, NVFP4_ERR_INVALID_ARG);
   NV_CHECK(out_aligned(y, y_dtype), NVFP4_ERR_MISALIGNED);
   NV_DEVICE();
-  NV_TRY(product(false, *qa, nullptr, 0, *qb, nullptr, 0, y, y_dtype, ldy, nullptr, static_cast<cudaStream_t>(stream)));
+  NV_TRY(product(*qa, nullptr, 0, *qb, nullptr, 0, y, y_dtype, ldy, nullptr, static_cast<cudaStream_t>(stream)));
   return NVFP4_OK;
 }
 
@@ -185,7 +181,8 @@ nvfp4_status mxfp4_gated_gemm(const mxfp4_tensor* qx, const mxfp4_tensor* q_gate
     NV_CHECK(out_aligned(y_or_null, y_dtype), NVFP4_ERR_MISALIGNED);
   }
   NV_DEVICE();
-  NV_TRY(product(false, *qx, nullptr, 0, *q_gate, q_up, act, y_or_null, y_dtype, ldy, qy_or_null, static_cast<cudaStream_t>(stream)));
+  NV_TRY(product(*qx, nullptr, 0, *q_gate, q_up, act, y_or_null, y_dtype, ldy, qy_or_null,
+                 static_cast<cudaStream_t>(stream)));
   return NVFP4_OK;
 }
 
@@ -206,7 +203,7 @@ nvfp4_status mxfp4_linear(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, 
   const mxfp4_tensor qx = carve(at, M, K);
   const bool fused = mx4_takes_bf16(M);
   if (!fused) NV_TRY(launch_mx4_quant(x, M, K, ldx, qx.codes, qx.scales, 1, nullptr, 0, s));
-  NV_TRY(product(!fused, qx, fused ? x : nullptr, ldx, *qw, nullptr, 0, y, y_dtype, ldy, nullptr, s));
+  NV_TRY(product(qx, fused ? x : nullptr, ldx, *qw, nullptr, 0, y, y_dtype, ldy, nullptr, s));
   return NVFP4_OK;
 }
 
@@ -233,11 +230,9 @@ nvfp4_status mxfp4_gated_mlp(const uint16_t* x, int64_t M, int64_t K, int64_t ld
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* at = static_cast<uint8_t*>(ws);
   const mxfp4_tensor qx = carve(at, M, K), qh = carve(at, M, F);
-  // (the gated kernel's weights load under the quantization: one token, cold
-  // weights, 18.9 us against 19.9 with X quantized in the gated kernel)
   NV_TRY(launch_mx4_quant(x, M, K, ldx, qx.codes, qx.scales, 1, nullptr, 0, s));
-  NV_TRY(product(true, qx, nullptr, 0, *q_gate, q_up, act, nullptr, 0, 0, &qh, s));
-  NV_TRY(product(true, qh, nullptr, 0, *q_down, nullptr, 0, y, y_dtype, ldy, nullptr, s));
+  NV_TRY(product(qx, nullptr, 0, *q_gate, q_up, act, nullptr, 0, 0, &qh, s));
+  NV_TRY(product(qh, nullptr, 0, *q_down, nullptr, 0, y, y_dtype, ldy, nullptr, s));
   return NVFP4_OK;
 }
 
@@ -315,7 +310,7 @@ nvfp4_status gated_linear_backward(const uint16_t* x, int64_t M, int64_t K, int6
   NV_TRY(launch_gated_slope(a, saved, dh, ld_dh, dg, du, s));
   if (dx_or_null != nullptr) NV_TRY(launch_gated_grad_x(a, dg, du, dx_or_null, ld_dx, s));
   if (dw_gate_or_null != nullptr || dw_up_or_null != nullptr)
-    NV_TRY(launch_gated_grad_w(a, dg, du, dw_gate_or_null, dw_up_or_null, dx_or_null != nullptr, s));
+    NV_TRY(launch_gated_grad_w(a, dg, du, dw_gate_or_null, dw_up_or_null, s));
   return NVFP4_OK;
 }
 

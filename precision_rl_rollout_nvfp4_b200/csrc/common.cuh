@@ -366,7 +366,10 @@ __device__ __host__ __forceinline__ int64_t scale_offset(int64_t row, int64_t bl
 // Programmatic dependent launch (kernels started by launch_k): pdl_wait()
 // returns once the previous kernel of the stream has completed and its
 // writes are visible; every thread calls it before its first global memory
-// access.  pdl_launch_dependents() lets the next kernel of the stream be
+// access (an L2 prefetch hint apart, which reads nothing into the SM).  No
+// kernel may rely on which kernel is queued before it: another host thread can
+// queue one on the same stream between two launches of one call.
+// pdl_launch_dependents() lets the next kernel of the stream be
 // scheduled (it then waits in its own pdl_wait()).  Both are no-ops for a
 // kernel launched without the attribute.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

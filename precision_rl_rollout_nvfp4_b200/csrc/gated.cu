@@ -54,7 +54,6 @@ struct Params {
   int row_tiles, col_tiles;    // 256-row tiles; 128 (forward) or 256 columns
   int steps, segments;         // K steps of 64 per segment
   int mats;                    // kGradW: matrices (1 or 2)
-  bool after;                  // kGradW: queued right after dX's product
   int act;
   uint16_t* out[2];
   int64_t ldo;
@@ -113,14 +112,8 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
   const uint32_t tmem = *slot;
   const int per_mat = p.row_tiles * p.col_tiles;
   const int total = per_mat * p.mats;
-  // The weights' gradients read dG, dU and X, which the kernels before the one
-  // just queued (dX, or dG and dU themselves when there is no dX) wrote: with
-  // p.after nothing is waited for until the end, and the two products share
-  // the SMs (see product() in api_mx4.cu for why those kernels are done).
-  if (MODE != kGradW || !p.after) {
-    pdl_wait();
-    pdl_launch_dependents();
-  }
+  pdl_wait();
+  pdl_launch_dependents();
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0;
@@ -273,10 +266,6 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
       acc_phase ^= 1u << buf;
       buf ^= 1;
     }
-  }
-  if (MODE == kGradW && p.after) {
-    pdl_wait();
-    pdl_launch_dependents();
   }
   fence_before();
   __syncthreads();
@@ -457,7 +446,7 @@ cudaError_t launch_gated_grad_x(const GatedArgs& a, const uint16_t* dg, const ui
 }
 
 cudaError_t launch_gated_grad_w(const GatedArgs& a, const uint16_t* dg, const uint16_t* du, uint16_t* dw_gate,
-                                uint16_t* dw_up, bool after_dx, cudaStream_t s) {
+                                uint16_t* dw_up, cudaStream_t s) {
   // the matrices asked for, in the order gate, up
   const uint16_t* from[2] = {dw_gate != nullptr ? dg : du, du};
   CUtensorMap m[4];
@@ -471,7 +460,6 @@ cudaError_t launch_gated_grad_w(const GatedArgs& a, const uint16_t* dg, const ui
   p.steps = static_cast<int>((a.M + 63) / 64);
   p.segments = 1;
   p.mats = (dw_gate != nullptr) + (dw_up != nullptr);
-  p.after = after_dx;
   p.out[0] = dw_gate != nullptr ? dw_gate : dw_up;
   p.out[1] = dw_up;
   p.ldo = a.K;

@@ -42,7 +42,6 @@ struct Mx4Gemm {
   const uint16_t* x_bf16;   // instead of x, for a plain product of mx4_takes_bf16 rows: quantized in the kernel
   int64_t ldx;
   int64_t M, N, K;
-  bool early;               // w and up are not written by the previous kernel of the stream: see pdl_wait
   int act;                  // kActSilu, kActGeluTanh
   int y_dtype;
   void* y;
@@ -72,12 +71,11 @@ cudaError_t launch_gated_forward(const GatedArgs& a, uint16_t* h, int64_t ldh, f
 // dG and dU (bf16 [M, F]) from the saved projections and dH.
 cudaError_t launch_gated_slope(const GatedArgs& a, const float* saved, const uint16_t* dh, int64_t ld_dh,
                                uint16_t* dg, uint16_t* du, cudaStream_t s);
-// dX [M, K], and dWg / dWu [F, K] (either may be null; after_dx: queued right
-// after launch_gated_grad_x on the stream).
+// dX [M, K], and dWg / dWu [F, K] (either may be null).
 cudaError_t launch_gated_grad_x(const GatedArgs& a, const uint16_t* dg, const uint16_t* du, uint16_t* dx,
                                 int64_t ld_dx, cudaStream_t s);
 cudaError_t launch_gated_grad_w(const GatedArgs& a, const uint16_t* dg, const uint16_t* du, uint16_t* dw_gate,
-                                uint16_t* dw_up, bool after_dx, cudaStream_t s);
+                                uint16_t* dw_up, cudaStream_t s);
 // Workspace bytes of gated_linear_backward.
 size_t gated_backward_ws(int64_t M, int64_t F, bool recompute);
 

@@ -77,7 +77,6 @@ struct SmallParams {
   const uint8_t* sf[3];          // scales of W, Up, X
   int64_t sf_row;                // bytes per 128-row block of a scale buffer
   int64_t sf_bytes[3];
-  bool early;                    // the weights may be read before the previous kernel's end
   void* y;
   int64_t ldy;
   bool pairs;                    // the rows of Y (fp32, bf16) take stores of column pairs
@@ -237,7 +236,7 @@ mx4_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
   const uint32_t tmem = *slot;
   const int atoms = static_cast<int>((p.K + 127) / 128);
   auto sf_n = [&](int k) { return (atoms - 2 * k >= 2 ? 2u : 1u) * kAtom; };
-  auto load_w = [&](int k, int stage) {              // opens the stage: its bytes are X's too
+  auto load = [&](int k, int stage) {
     const uint32_t fb = smem_u32(&full[stage]), n = sf_n(k);
     uint8_t* st = smem + stage * DATA;
     uint8_t* sf = sf_base + stage * C::SF;
@@ -249,30 +248,20 @@ mx4_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     if (GATED) tma_load_2d(smem_u32(st + kWTile), &tmU, k * kRowBytes, nt * kTile, fb);
     bulk_load(smem_u32(sf), p.sf[0] + off, n, fb);
     if (GATED) bulk_load(smem_u32(sf + 2 * kAtom), p.sf[1] + off, n, fb);
+    if (!XQ) {
+      tma_load_2d(smem_u32(st + C::NW * kWTile), &tmX, k * kRowBytes, static_cast<int>(t0), fb);
+      bulk_load(smem_u32(sf + C::NW * 2 * kAtom), p.sf[2] + (t0 >> 7) * p.sf_row + 2ll * k * kAtom, n, fb);
+    }
     return true;
   };
-  auto load_x = [&](int k, int stage) {
-    if (XQ) return;
-    const uint32_t fb = smem_u32(&full[stage]);
-    tma_load_2d(smem_u32(smem + stage * DATA + C::NW * kWTile), &tmX, k * kRowBytes,
-                static_cast<int>(t0), fb);
-    bulk_load(smem_u32(sf_base + stage * C::SF + C::NW * 2 * kAtom), p.sf[2] + (t0 >> 7) * p.sf_row + 2ll * k * kAtom,
-              sf_n(k), fb);
-  };
-  // Before the previous kernel's end: the first stages' weights, where they
-  // are known not to be that kernel's output (one token through the gated
-  // block: 20.6 -> 19.5 us), else a hint to bring them into L2 (gated, cold:
-  // 11.5 -> 10.7 us; for more than the first steps it delays them).
-  int pre = 0;
+  // Before the previous kernel's end, a hint to bring the first steps' weights
+  // into L2 (gated, cold: 11.5 -> 10.7 us; for more steps it delays them).  They
+  // are not loaded here, even where the kernel before is the same call's
+  // quantizer: another host thread may queue a kernel that writes them in between.
   if (warp == 0 && lane == 0) {
-    if (p.early) {
-      for (; pre < C::STAGES && k_lo + pre < k_hi; ++pre)
-        if (!load_w(k_lo + pre, pre)) break;
-    } else {
-      for (int k = k_lo; k < k_hi && k < k_lo + 4; ++k) {
-        prefetch_2d(&tmW, k * kRowBytes, nt * kTile);
-        if (GATED) prefetch_2d(&tmU, k * kRowBytes, nt * kTile);
-      }
+    for (int k = k_lo; k < k_hi && k < k_lo + 4; ++k) {
+      prefetch_2d(&tmW, k * kRowBytes, nt * kTile);
+      if (GATED) prefetch_2d(&tmU, k * kRowBytes, nt * kTile);
     }
   }
   pdl_wait();
@@ -283,8 +272,7 @@ mx4_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
       int stage = 0;
       uint32_t phase = 0, armed = 0, armed_phase = 0;
       for (int k = k_lo; k < k_hi; ++k) {
-        if (k - k_lo >= pre && (!mbar_wait(&empty[stage], phase ^ 1, p.err) || !load_w(k, stage))) break;
-        load_x(k, stage);
+        if (!mbar_wait(&empty[stage], phase ^ 1, p.err) || !load(k, stage)) break;
         armed |= 1u << stage;
         armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
         if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
@@ -483,7 +471,6 @@ cudaError_t launch_small(const Mx4Gemm& g, cudaStream_t s) {
   p.K = g.K;
   p.steps = static_cast<int>((g.K + kStepK - 1) / kStepK);
   p.last = static_cast<int>((g.K - (p.steps - 1ll) * kStepK + 63) / 64);
-  p.early = g.early;
   p.x = g.x_bf16;
   p.ldx = g.ldx;
   p.sf_row = (g.K + 127) / 128 * kAtom;

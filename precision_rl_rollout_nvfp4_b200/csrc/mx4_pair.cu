@@ -53,7 +53,6 @@ struct PairParams {
   int64_t M, N, K;
   int row_tiles, col_tiles, steps;
   int last;                      // K = 64 products of the last step
-  bool early;                    // the weights may be read before the previous kernel's end
   void* y;
   int64_t ldy;
   bool vec;                      // y rows can take 16-byte stores
@@ -272,36 +271,27 @@ mx4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   fence_after();
   const uint32_t tmem = *slot_word;
   const int total = p.row_tiles * p.col_tiles;
-  // this CTA's loads of a K step: B and its scales (which open the stage), A
-  // and its scales
-  auto load_b = [&](int ct, int k, int stage) {
+  // this CTA's loads of a K step: B and its scales, A and its scales
+  auto load = [&](int rt, int ct, int k, int stage) {
     if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kStage);
     const uint32_t bar = peer_u32(smem_u32(&full[stage]), 0);
-    const uint32_t b = smem_u32(smem + stage * 2 * kOperand) + kOperand;
-    const uint32_t s = smem_u32(sf + stage * (kSfA + kSfB)) + kSfA;
+    const uint32_t a = smem_u32(smem + stage * 2 * kOperand), b = a + kOperand;
+    const uint32_t sa = smem_u32(sf + stage * (kSfA + kSfB)), s = sa + kSfA;
     load_2d_pair(b, GATED && rank ? &tmB1 : &tmB0, k * kRowBytes, (GATED ? ct : 2 * ct + static_cast<int>(rank)) * 128,
                  bar);
     load_2d_pair(s, &tmSB0, k * kSfA / 8, GATED ? ct : 2 * ct, bar);
     load_2d_pair(s + kSfA, GATED ? &tmSB1 : &tmSB0, k * kSfA / 8, GATED ? ct : 2 * ct + 1, bar);
-  };
-  auto load_a = [&](int rt, int k, int stage) {
-    const uint32_t bar = peer_u32(smem_u32(&full[stage]), 0);
     const int block = 2 * rt + static_cast<int>(rank);       // 128-row block
-    load_2d_pair(smem_u32(smem + stage * 2 * kOperand), &tmA, k * kRowBytes, block * 128, bar);
-    load_2d_pair(smem_u32(sf + stage * (kSfA + kSfB)), &tmSA, k * kSfA / 8, block, bar);
+    load_2d_pair(a, &tmA, k * kRowBytes, block * 128, bar);
+    load_2d_pair(sa, &tmSA, k * kSfA / 8, block, bar);
   };
-  // before the previous kernel's end: the first stages' weights, where they are
-  // known not to be that kernel's output, else a hint to bring them into L2
-  int pre = 0;
+  // before the previous kernel's end: a hint to bring the first steps' weights
+  // into L2 (no load, which could meet a write queued by another host thread)
   if (warp == 0 && lane == 0 && pair < total) {
     int rt, ct;
     tile_at(pair, p.row_tiles, p.col_tiles, rt, ct);
-    if (p.early) {
-      for (; pre < kStages && pre < p.steps; ++pre) load_b(ct, pre, pre);
-    } else {
-      for (int k = 0; k < kStages && k < p.steps; ++k)
-        prefetch_2d(GATED && rank ? &tmB1 : &tmB0, k * kRowBytes, (GATED ? ct : 2 * ct + static_cast<int>(rank)) * 128);
-    }
+    for (int k = 0; k < kStages && k < p.steps; ++k)
+      prefetch_2d(GATED && rank ? &tmB1 : &tmB0, k * kRowBytes, (GATED ? ct : 2 * ct + static_cast<int>(rank)) * 128);
   }
   pdl_wait();
   pdl_launch_dependents();
@@ -315,13 +305,8 @@ mx4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         int rt, ct;
         tile_at(tile, p.row_tiles, p.col_tiles, rt, ct);
         for (int k = 0; k < p.steps; ++k) {
-          if (pre > 0) {
-            --pre;                                           // this step's B is on its way already
-          } else {
-            if (!mbar_wait(&empty[stage], phase ^ 1, p.err)) { ok = false; break; }
-            load_b(ct, k, stage);
-          }
-          load_a(rt, k, stage);
+          if (!mbar_wait(&empty[stage], phase ^ 1, p.err)) { ok = false; break; }
+          load(rt, ct, k, stage);
           armed |= 1u << stage;
           armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
           if (++stage == kStages) { stage = 0; phase ^= 1; }
@@ -478,7 +463,6 @@ cudaError_t launch(const Mx4Gemm& g, cudaStream_t s) {
   p.col_tiles = static_cast<int>((g.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256));
   p.steps = static_cast<int>((g.K + kStepK - 1) / kStepK);
   p.last = static_cast<int>((g.K - (p.steps - 1ll) * kStepK + 63) / 64);
-  p.early = g.early;
   p.y = g.y;
   p.ldy = g.ldy;
   p.vec = (reinterpret_cast<uintptr_t>(g.y) & 15u) == 0 && g.ldy % (OUT == 0 ? 4 : 8) == 0;
