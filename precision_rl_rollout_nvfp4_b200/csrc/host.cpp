@@ -127,6 +127,24 @@ int64_t attr_int(PyObject* o, PyObject* name) {
   if (n == -1 && PyErr_Occurred()) throw python_error();
   return n;
 }
+
+// Integer and truth arguments: converted first of all in every call, since the
+// conversion may run Python code or raise, for which the interpreter's lock has
+// to be held.
+int as_int(PyObject* o) {
+  const long n = PyLong_AsLong(o);
+  if (n == -1 && PyErr_Occurred()) throw python_error();
+  if (n != static_cast<int>(n)) {
+    PyErr_SetString(PyExc_OverflowError, "integer argument out of range");
+    throw python_error();
+  }
+  return static_cast<int>(n);
+}
+bool as_bool(PyObject* o) {
+  const int n = PyObject_IsTrue(o);
+  if (n < 0) throw python_error();
+  return n != 0;
+}
 Tensor attr_tensor(PyObject* o, PyObject* name, const char* where) {
   PyObject* v = PyObject_GetAttr(o, name);
   if (v == nullptr) throw python_error();
@@ -225,13 +243,13 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HOST_BEGIN
   WANT(4)
   const char* where = "mxfp4_quantize";
+  const int layout = as_int(a[1]);
+  const bool values = as_bool(a[3]);
   const Tensor& x = tensor(a[0], where);
   const Rows r = rows(x, where);
   const c10::cuda::CUDAGuard guard(x.device());
-  const int layout = static_cast<int>(PyLong_AsLong(a[1]));
   Mx q = a[2] == Py_None ? mx_empty(r.M, r.K, layout, x) : mx(a[2], where);
   on_device(q.codes, x, where);
-  const bool values = a[3] == Py_True;
   Tensor v = values ? empty(x.sizes(), at::kBFloat16, x) : Tensor();
   nvfp4_status st;
   {
@@ -269,9 +287,10 @@ PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HOST_BEGIN
   WANT(3)
   const char* where = "mxfp4_dequantize";
+  const int code = as_int(a[1]);
   const Mx q = mx(a[0], where);
   const c10::cuda::CUDAGuard guard(q.codes.device());
-  const Out y = output(a[2], {q.c.rows}, q.c.cols, static_cast<int>(PyLong_AsLong(a[1])), q.codes, where);
+  const Out y = output(a[2], {q.c.rows}, q.c.cols, code, q.codes, where);
   nvfp4_status st;
   {
     NoGil g;
@@ -287,10 +306,11 @@ PyObject* gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HOST_BEGIN
   WANT(4)
   const char* where = "mxfp4_gemm";
+  const int code = as_int(a[2]);
   const Mx qa = mx(a[0], where), qb = mx(a[1], where);
   on_device(qb.codes, qa.codes, where);
   const c10::cuda::CUDAGuard guard(qa.codes.device());
-  const Out y = output(a[3], {qa.c.rows}, qb.c.rows, static_cast<int>(PyLong_AsLong(a[2])), qa.codes, where);
+  const Out y = output(a[3], {qa.c.rows}, qb.c.rows, code, qa.codes, where);
   nvfp4_status st;
   {
     NoGil g;
@@ -306,11 +326,11 @@ PyObject* gated_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HOST_BEGIN
   WANT(6)
   const char* where = "mxfp4_gated_gemm";
+  const int act = as_int(a[3]), code = as_int(a[4]);
   const Mx x = mx(a[0], where), g = mx(a[1], where), u = mx(a[2], where);
   on_device(g.codes, x.codes, where);
   on_device(u.codes, x.codes, where);
   const c10::cuda::CUDAGuard guard(x.codes.device());
-  const int act = static_cast<int>(PyLong_AsLong(a[3])), code = static_cast<int>(PyLong_AsLong(a[4]));
   nvfp4_status st;
   if (code == 2) {
     Mx q = a[5] == Py_None ? mx_empty(x.c.rows, g.c.rows, 1, x.codes) : mx(a[5], where);
@@ -337,12 +357,13 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HOST_BEGIN
   WANT(4)
   const char* where = "mxfp4_linear";
+  const int code = as_int(a[2]);
   const Tensor& x = tensor(a[0], where);
   const Rows r = rows(x, where);
   const Mx w = mx(a[1], where);
   on_device(w.codes, x, where);
   const c10::cuda::CUDAGuard guard(x.device());
-  const Out y = output(a[3], x.sizes().slice(0, x.dim() - 1), w.c.rows, static_cast<int>(PyLong_AsLong(a[2])), x, where);
+  const Out y = output(a[3], x.sizes().slice(0, x.dim() - 1), w.c.rows, code, x, where);
   const size_t bytes = api.workspace(NVFP4_OP_MXFP4_LINEAR, r.M, 0, r.K, 1);
   const Tensor ws = empty({static_cast<int64_t>(bytes)}, at::kByte, x);
   nvfp4_status st;
@@ -360,6 +381,7 @@ PyObject* mlp(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HOST_BEGIN
   WANT(7)
   const char* where = "mxfp4_gated_mlp";
+  const int act = as_int(a[4]), code = as_int(a[5]);
   const Tensor& x = tensor(a[0], where);
   const Rows r = rows(x, where);
   const Mx g = mx(a[1], where), u = mx(a[2], where), d = mx(a[3], where);
@@ -367,14 +389,13 @@ PyObject* mlp(PyObject*, PyObject* const* a, Py_ssize_t n) {
   on_device(u.codes, x, where);
   on_device(d.codes, x, where);
   const c10::cuda::CUDAGuard guard(x.device());
-  const Out y = output(a[6], x.sizes().slice(0, x.dim() - 1), d.c.rows, static_cast<int>(PyLong_AsLong(a[5])), x, where);
+  const Out y = output(a[6], x.sizes().slice(0, x.dim() - 1), d.c.rows, code, x, where);
   const size_t bytes = api.workspace(NVFP4_OP_MXFP4_MLP, r.M, g.c.rows, r.K, 1);
   const Tensor ws = empty({static_cast<int64_t>(bytes)}, at::kByte, x);
   nvfp4_status st;
   {
     NoGil ng;
-    st = api.mlp(r.p(), r.M, r.K, r.ld, &g.c, &u.c, &d.c, static_cast<int>(PyLong_AsLong(a[4])), y.t.data_ptr(), y.code,
-                 y.ld, ws.data_ptr(), bytes, stream_of(x));
+    st = api.mlp(r.p(), r.M, r.K, r.ld, &g.c, &u.c, &d.c, act, y.t.data_ptr(), y.code, y.ld, ws.data_ptr(), bytes, stream_of(x));
   }
   check(st, where);
   return THPVariable_Wrap(y.t);
@@ -448,14 +469,15 @@ void backward_call(const Tensor& x, const Tensor& wg, const Tensor& wu, const Te
 PyObject* gated_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HOST_BEGIN
   WANT(5)
+  const int act = as_int(a[3]);
+  const bool save = as_bool(a[4]);
   const Tensor &x = tensor(a[0], "gated_linear_forward"), &g = tensor(a[1], "gated_linear_forward"),
                &u = tensor(a[2], "gated_linear_forward");
   TORCH_CHECK_VALUE(x.is_cuda(), "gated_linear_forward: expected CUDA tensors");
   const c10::cuda::CUDAGuard guard(x.device());
   const at::NoGradGuard no_grad;
   Tensor saved;
-  const bool save = a[4] == Py_True;
-  Tensor h = forward_call(x, g, u, static_cast<int>(PyLong_AsLong(a[3])), save, &saved);
+  Tensor h = forward_call(x, g, u, act, save, &saved);
   return save ? Py_BuildValue("(NN)", THPVariable_Wrap(h), THPVariable_Wrap(saved)) : THPVariable_Wrap(h);
   HOST_END
 }
@@ -465,16 +487,17 @@ PyObject* gated_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HOST_BEGIN
   WANT(7)
   const char* where = "gated_linear_backward";
+  const int act = as_int(a[4]);
+  TORCH_CHECK_VALUE(PyTuple_Check(a[6]) && PyTuple_GET_SIZE(a[6]) == 3, where, ": need is a tuple of three");
+  bool need[3];
+  for (int i = 0; i < 3; ++i) need[i] = as_bool(PyTuple_GET_ITEM(a[6], i));
   const Tensor &x = tensor(a[0], where), &g = tensor(a[1], where), &u = tensor(a[2], where), &dh = tensor(a[3], where);
   TORCH_CHECK_VALUE(x.is_cuda(), where, ": expected CUDA tensors");
   const c10::cuda::CUDAGuard guard(x.device());
   const at::NoGradGuard no_grad;
   const Tensor saved = a[5] == Py_None ? Tensor() : tensor(a[5], where);
-  TORCH_CHECK_VALUE(PyTuple_Check(a[6]) && PyTuple_GET_SIZE(a[6]) == 3, where, ": need is a tuple of three");
-  bool need[3];
-  for (int i = 0; i < 3; ++i) need[i] = PyObject_IsTrue(PyTuple_GET_ITEM(a[6], i)) == 1;
   Tensor grad[3];
-  backward_call(x, g, u, dh, static_cast<int>(PyLong_AsLong(a[4])), saved, need, grad);
+  backward_call(x, g, u, dh, act, saved, need, grad);
   PyObject* r = PyTuple_New(3);
   for (int i = 0; i < 3; ++i) PyTuple_SET_ITEM(r, i, THPVariable_Wrap(grad[i]));   // (undefined: None)
   return r;
@@ -580,13 +603,14 @@ PyObject* gated_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HOST_BEGIN
   WANT(8)
   const char* where = "gated_linear";
+  const int act = as_int(a[3]), fmt = as_int(a[5]);
+  const bool recompute = as_bool(a[4]), act_quant = as_bool(a[6]), enabled = as_bool(a[7]);
   const Tensor &x = tensor(a[0], where), &g = tensor(a[1], where), &u = tensor(a[2], where);
   TORCH_CHECK_VALUE(x.is_cuda(), where, ": expected CUDA tensors");
   const c10::cuda::CUDAGuard guard(x.device());
-  const bool grads = a[7] == Py_True && (x.requires_grad() || g.requires_grad() || u.requires_grad());
+  const bool grads = enabled && (x.requires_grad() || g.requires_grad() || u.requires_grad());
   if (grads) check_capture({&x, &g, &u}, where);
-  return THPVariable_Wrap(GatedLinear::apply(x, g, u, PyLong_AsLong(a[3]), grads && a[4] != Py_True,
-                                             PyLong_AsLong(a[5]), a[6] == Py_True));
+  return THPVariable_Wrap(GatedLinear::apply(x, g, u, act, grads && !recompute, fmt, act_quant));
   HOST_END
 }
 
