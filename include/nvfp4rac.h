@@ -475,7 +475,9 @@ nvfp4_status mxfp4_gated_mlp(const uint16_t* x, int64_t M, int64_t K, int64_t ld
  *   dWg = dG^T X, dWu = dU^T X
  * x [M, K], w_gate and w_up [F, K] (one row stride ldw), h and dh [M, F], dx
  * [M, K], dw_* [F, K] contiguous; K % 8 == F % 8 == 0, any M >= 0 (with M ==
- * 0 the weights' gradients are zero).  Products accumulate in fp32; H and the
+ * 0 the weights' gradients are zero).  A reduction has at most 2^26 terms: K
+ * <= 2^26, and F <= 2^25 for dx and M <= 2^26 for dw_* (longer ones:
+ * NVFP4_ERR_UNSUPPORTED_SHAPE).  Products accumulate in fp32; H and the
  * gradients are rounded once, dG and dU once on their way to the products.
  *   saved: gated_linear_saved_bytes(M, F) bytes, G and U in fp32 in a layout of
  *   the library's own, written by the forward call (NULL: nothing is kept) and

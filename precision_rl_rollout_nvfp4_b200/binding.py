@@ -678,7 +678,8 @@ def gated_linear(x, w_gate, w_up, act="silu", recompute=False):
     autograd: both projections, the activation and the product in one kernel,
     their gradients in three.  The forward pass keeps the two projections in
     fp32 (8 bytes per output); recompute=True keeps nothing and computes them
-    again in the backward pass.  A call under stream capture is refused while
+    again in the backward pass.  K <= 2^26; gradients need F <= 2^25 (x) and at
+    most 2^26 rows (weights).  A call under stream capture is refused while
     an eager graph of the same leaves, built on the default stream, lives."""
     return _host.gated_linear(x, w_gate, w_up, _activation(act), bool(recompute), 0, False, torch.is_grad_enabled())
 
