@@ -18,14 +18,31 @@ from __future__ import annotations
 import argparse
 
 
+BLOCK_CALLS = ("mxfp4_quantize", "mxfp4_dequantize", "mxfp4_qdq", "mxfp4_gemm", "mxfp4_linear", "mxfp4_gated_gemm",
+               "mxfp4_gated_mlp", "gated_forward", "gated_backward")
+
+
 def block_calls(B, S, a, dev, names):
-    """The MXFP4 and gated calls among `names`, on synthetic inputs."""
+    """The MXFP4 and gated calls among `names`, on synthetic inputs; the operands
+    that only other calls take are not made."""
     import torch
+    names = [n for n in names if n in BLOCK_CALLS]
+    if not names:
+        return {}
+
+    def needs(*calls):
+        return any(n in calls for n in names)
+
     x = S.activations(a.M, a.K).to(dev)
     wg, wu = S.weights(a.N, a.K, seed=1).to(dev), S.weights(a.N, a.K, seed=2).to(dev)
-    wd = S.weights(a.K, a.N, seed=3).to(dev)
-    qx, qg, qu, qd = (B.mxfp4_quantize(t) for t in (x, wg, wu, wd))
-    dh = S.activations(a.M, a.N, seed=4).to(dev)
+    if needs("mxfp4_dequantize", "mxfp4_gemm", "mxfp4_gated_gemm"):
+        qx = B.mxfp4_quantize(x)
+    if needs("mxfp4_gemm", "mxfp4_linear", "mxfp4_gated_gemm", "mxfp4_gated_mlp"):
+        qg, qu = B.mxfp4_quantize(wg), B.mxfp4_quantize(wu)
+    if needs("mxfp4_gated_mlp"):
+        qd = B.mxfp4_quantize(S.weights(a.K, a.N, seed=3).to(dev))
+    if needs("gated_backward"):
+        dh = S.activations(a.M, a.N, seed=4).to(dev)
     y_dtype = torch.bfloat16 if a.y_dtype == "bf16" else torch.float32
     saved = []
     fns = {"mxfp4_quantize": lambda: B.mxfp4_quantize(x), "mxfp4_dequantize": lambda: B.mxfp4_dequantize(qx),
@@ -35,7 +52,7 @@ def block_calls(B, S, a, dev, names):
            "mxfp4_gated_mlp": lambda: B.mxfp4_gated_mlp(x, qg, qu, qd, out_dtype=y_dtype),
            "gated_forward": lambda: saved.append(B.gated_linear_forward(x, wg, wu, save=True)[1]),
            "gated_backward": lambda: B.gated_linear_backward(x, wg, wu, dh, saved=saved[-1] if saved else None)}
-    return {n: fns[n] for n in names if n in fns}
+    return {n: fns[n] for n in names}
 
 
 def main(argv=None):
