@@ -2,8 +2,8 @@
 
 Argument marshalling only: torch provides device memory and the current
 stream; every step of the path runs in the library's CUDA kernels.  Importing
-this module fails loudly when the library is missing -- there is no CPU
-fallback.
+this module fails loudly when the library is missing, and the MXFP4 and gated
+calls when the native host module is -- there is no CPU fallback.
 """
 from __future__ import annotations
 
@@ -518,18 +518,28 @@ def w8a8_gemm(qa, qb, out_dtype=torch.float32, out=None, stream=None):
 # These calls are short on the GPU (a few microseconds for one token), so their
 # host side (checks, allocation on the current stream, the C call, the autograd
 # node) is native: csrc/host.cpp.
-try:
-    from . import _host
-except ImportError as e:
-    raise ImportError("the _host module is missing or does not load: build it with "
-                      "`python -m precision_rl_rollout_nvfp4_b200.build_lib`") from e
-
-
 def _raise_status(status, where):
     raise NvFP4Error(status, where)
 
 
-_host.init({n: ctypes.cast(getattr(_lib, n), P).value for n in EXPORTS}, _raise_status)
+class _NoHost:
+    """Stands for a host module that does not load (it is built against one
+    version of torch): each call that needs it raises; the others, which go
+    through ctypes, run."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError("the _host module, which this call needs, is missing or does not load: build it with "
+                          "`python -m precision_rl_rollout_nvfp4_b200.build_lib`") from self._why
+
+
+try:
+    from . import _host
+    _host.init({n: ctypes.cast(getattr(_lib, n), P).value for n in EXPORTS}, _raise_status)
+except ImportError as _e:
+    _host = _NoHost(_e)
 _Y_DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 _FMT = {"nvfp4": 1, "mxfp4": 2}
 
