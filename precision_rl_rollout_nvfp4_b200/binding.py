@@ -13,6 +13,8 @@ from dataclasses import dataclass
 
 import torch
 
+from .build_lib import host_target
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # NVFP4_LIB=checked loads the index-checked build (libnvfp4rac_checked.so)
 LIB_PATH = os.path.join(_PKG, "libnvfp4rac_checked.so" if os.environ.get("NVFP4_LIB") == "checked"
@@ -537,6 +539,8 @@ class _NoHost:
 
 try:
     from . import _host
+    if _host.built_against != host_target():
+        raise ImportError(f"_host is built against {_host.built_against}, this is {host_target()}")
     _host.init({n: ctypes.cast(getattr(_lib, n), P).value for n in EXPORTS}, _raise_status)
 except ImportError as _e:
     _host = _NoHost(_e)

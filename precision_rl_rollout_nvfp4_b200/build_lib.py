@@ -6,6 +6,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
@@ -34,12 +35,29 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def build_host(force: bool = False) -> str:
+def host_target() -> str:
+    """What a host module has to be built against to serve this interpreter."""
+    import torch
+    return f"torch {torch.__version__} python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
+def host_needs_build(path: str = HOST) -> bool:
+    """Missing, older than its sources, or built against another torch or Python
+    (the module carries the name of what it was built against)."""
+    if not os.path.exists(path):
+        return True
     src = os.path.join(PKG, "csrc", "host.cpp")
     header = os.path.join(ROOT, "include", "nvfp4rac.h")
-    if (not force and os.path.exists(HOST)
-            and os.path.getmtime(HOST) > max(os.path.getmtime(src), os.path.getmtime(header))):
+    if os.path.getmtime(path) <= max(os.path.getmtime(src), os.path.getmtime(header)):
+        return True
+    with open(path, "rb") as f:
+        return host_target().encode() + b"\0" not in f.read()
+
+
+def build_host(force: bool = False) -> str:
+    if not force and not host_needs_build():
         return HOST
+    src = os.path.join(PKG, "csrc", "host.cpp")
     import torch
     from torch.utils.cpp_extension import include_paths
     cuda = os.path.dirname(os.path.dirname(nvcc()))
@@ -49,7 +67,8 @@ def build_host(force: bool = False) -> str:
     # the system's g++, as nvcc takes it: a compiler that links its own libstdc++
     # statically gives the module a second one next to torch's
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in inc), src, "-o",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DHOST_BUILT_AGAINST="{host_target()}"', *(f"-I{i}" for i in inc), src, "-o",
            HOST + ".tmp", f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-ltorch", "-ltorch_cuda", "-lc10", "-lc10_cuda",
            f"-Wl,-rpath,{lib}"]
     res = subprocess.run(cmd, capture_output=True, text=True)
