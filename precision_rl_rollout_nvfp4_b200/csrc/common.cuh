@@ -64,6 +64,15 @@ __device__ __forceinline__ bool idx_ok(bool ok, unsigned line) {
   }
 #endif
 
+// Whether n elements from (row, col) on lie in a matrix of row stride ld: by
+// their offset against the matrix's end, so that a check says more than the
+// comparison of row and column that guards the access.
+__device__ __host__ __forceinline__ bool in_matrix(int64_t row, int64_t col, int64_t n, int64_t rows, int64_t cols,
+                                                   int64_t ld) {
+  const int64_t at = row * ld + col;
+  return at >= 0 && col + n <= ld && at + n <= (rows - 1) * ld + cols;
+}
+
 // Bytes of a scale buffer of rows x cols with blocks of `blk` elements in
 // `layout` (0 canonical, 1 MMA-tiled with 128-row blocks of 4-block atoms).
 __device__ __host__ __forceinline__ int64_t scale_extent(int64_t rows, int64_t cols, int layout, int blk) {

@@ -226,7 +226,8 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             tmem_ld(trow + 128 + at, u);
             tmem_ld_wait(v, u);
             const int64_t rb = row0 / 32, cb = (col0 + at) / 32;
-            if (p.saved != nullptr && rb < p.sv_rb && cb < p.sv_cb) {
+            if (p.saved != nullptr && rb < p.sv_rb && cb < p.sv_cb &&
+                NV_IDX(saved_at(rb, cb, p.sv_cb) + 1024 <= p.sv_rb * p.sv_cb * 1024)) {
               float* g = p.saved + saved_at(rb, cb, p.sv_cb) + 4 * lane;
               float* w = g + p.sv_rb * p.sv_cb * 1024;
 #pragma unroll
@@ -257,7 +258,7 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int rr = 4 * i + (lane >> 3);
-          if (row0 + rr < p.rows && col < p.cols && NV_IDX(row0 + rr < p.rows && col + 8 <= p.cols))
+          if (row0 + rr < p.rows && col < p.cols && NV_IDX(in_matrix(row0 + rr, col, 8, p.rows, p.cols, p.ldo)))
             *reinterpret_cast<uint4*>(out + (row0 + rr) * p.ldo + col) =
                 *reinterpret_cast<const uint4*>(stg_warp + rr * kStgStride + 16 * (lane & 7));
         }
@@ -323,7 +324,7 @@ gated_slope_kernel(const float* __restrict__ saved, int64_t n_rb, int64_t n_cb, 
       const int rr = 8 * i + (lane >> 2);
       const int64_t row = rb * 32 + rr;
       uint4 v = make_uint4(0, 0, 0, 0);
-      if (row < M && col < F) v = ld_nc_v4(dh + row * ld_dh + col);
+      if (row < M && col < F && NV_IDX(in_matrix(row, col, 8, M, F, ld_dh))) v = ld_nc_v4(dh + row * ld_dh + col);
       *reinterpret_cast<uint4*>(t0 + rr * kBwdStride + 16 * (lane & 3)) = v;
     }
     __syncwarp();
@@ -350,7 +351,7 @@ gated_slope_kernel(const float* __restrict__ saved, int64_t n_rb, int64_t n_cb, 
     for (int i = 0; i < 4; ++i) {
       const int rr = 8 * i + (lane >> 2);
       const int64_t row = rb * 32 + rr;
-      if (row < M && col < F && NV_IDX(row < M && col + 8 <= F)) {
+      if (row < M && col < F && NV_IDX(in_matrix(row, col, 8, M, F, F))) {
         *reinterpret_cast<uint4*>(dg + row * F + col) = *reinterpret_cast<const uint4*>(t0 + rr * kBwdStride + 16 * (lane & 3));
         *reinterpret_cast<uint4*>(du + row * F + col) = *reinterpret_cast<const uint4*>(t1 + rr * kBwdStride + 16 * (lane & 3));
       }

@@ -133,7 +133,7 @@ mx4_quant_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t prows, ui
     const uint32_t col = it.seg * 512 + 16 * lane;
     const bool in = row < rows && col < K;                    // K % 32 == 0: a block is in or out
     uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (in) load32<WIDE>(x + row * ldx + col, w);
+    if (in && NV_IDX(in_matrix(row, col, 16, rows, K, ldx))) load32<WIDE>(x + row * ldx + col, w);
     uint32_t m2 = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(w[0], w[1]), bf16x2_absmax(w[2], w[3])),
                                 bf16x2_absmax(bf16x2_absmax(w[4], w[5]), bf16x2_absmax(w[6], w[7])));
     m2 = bf16x2_absmax(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, 1));         // the block's other half
@@ -152,7 +152,7 @@ mx4_quant_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t prows, ui
       out[h] = bad ? 0u : e2m1x8_f2(p);
     }
     if (CODES) {
-      if (in && NV_IDX(row < rows && col + 16 <= K))
+      if (in && NV_IDX(in_matrix(row, col / 2, 8, rows, K / 2, K / 2)))
         *reinterpret_cast<uint2*>(codes + row * (K / 2) + col / 2) = make_uint2(out[0], out[1]);
       if (layout == 1) {
         // the four blocks' scales of an atom as one word
@@ -162,11 +162,11 @@ mx4_quant_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t prows, ui
         const uint32_t atom = it.seg * 4 + (lane >> 3);
         if (sub == 0 && atom < atoms && NV_IDX(tiled_word(row, atom, atoms) + 4 <= scale_extent(rows, K, 1, 32)))
           *reinterpret_cast<uint32_t*>(scales + tiled_word(row, atom, atoms)) = word;
-      } else if (in && (lane & 1) == 0 && NV_IDX(row < rows && col < K)) {
+      } else if (in && (lane & 1) == 0 && NV_IDX(in_matrix(row, col / 32, 1, rows, K / 32, K / 32))) {
         scales[row * (K / 32) + col / 32] = static_cast<uint8_t>(sb);
       }
     }
-    if (QDQ && in && NV_IDX(row < rows && col + 16 <= K)) {
+    if (QDQ && in && NV_IDX(in_matrix(row, col, 16, rows, K, ldo))) {
       const uint32_t s = scale_bf16x2(sb);
       uint32_t v[8];
       e2m1x8_bf16(out[0], v);
@@ -191,11 +191,12 @@ mx4_dequant_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict_
   for (Units it(rows, segs); it.more(); it.next()) {
     const int64_t row = it.row;
     const uint32_t col = it.seg * 512 + 16 * lane;
-    if (col >= K || !NV_IDX(row < rows)) continue;
+    if (col >= K) continue;
+    if (!NV_IDX(in_matrix(row, col / 2, 8, rows, K / 2, K / 2) && in_matrix(row, col, 16, rows, K, ldy))) continue;
     const uint2 c = *reinterpret_cast<const uint2*>(codes + row * (K / 2) + col / 2);
     const int64_t off = layout == 1 ? tiled_word(row, it.seg * 4 + (lane >> 3), atoms) + ((lane & 7) >> 1)
                                     : row * (K / 32) + col / 32;
-    const uint32_t s = scale_bf16x2(scales[off]);
+    const uint32_t s = scale_bf16x2(NV_IDX(off < scale_extent(rows, K, layout, 32)) ? scales[off] : 255u);
     uint32_t v[8];
     e2m1x8_bf16(c.x, v);
     e2m1x8_bf16(c.y, v + 4);

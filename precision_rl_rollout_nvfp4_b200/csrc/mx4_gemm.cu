@@ -98,30 +98,32 @@ __device__ __forceinline__ void store_lanes(const SmallParams& p, int64_t t, int
     // columns of one of them (777 x 2048 x 1024: 6.4 -> 5.8 us)
     const int odd = threadIdx.x & 1;
     uint16_t* y = static_cast<uint16_t*>(p.y) + (t + odd) * p.ldy + (n - odd);
-    const bool in = n < p.N && NV_IDX(t < p.M);
+    const bool in = n < p.N;
 #pragma unroll
     for (int i = 0; i < CNT; i += 2) {
       const uint32_t w = bf16x2(v[i], v[i + 1]);                // tokens t + i (low half), t + i + 1
       const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w, 1);
-      if (in && i + odd < count) *reinterpret_cast<uint32_t*>(y) = odd ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
+      if (in && i + odd < count && NV_IDX(in_matrix(t + odd + i, n - odd, 2, p.M, p.N, p.ldy)))
+        *reinterpret_cast<uint32_t*>(y) = odd ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
       y += 2 * p.ldy;
     }
   } else if (OUT == 0 && p.pairs) {
     const int odd = threadIdx.x & 1;
     float* y = static_cast<float*>(p.y) + (t + odd) * p.ldy + (n - odd);
-    const bool in = n < p.N && NV_IDX(t < p.M);
+    const bool in = n < p.N;
 #pragma unroll
     for (int i = 0; i < CNT; i += 2) {
       const float o = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[i] : v[i + 1], 1);
-      if (in && i + odd < count) *reinterpret_cast<float2*>(y) = odd ? make_float2(o, v[i + 1]) : make_float2(v[i], o);
+      if (in && i + odd < count && NV_IDX(in_matrix(t + odd + i, n - odd, 2, p.M, p.N, p.ldy)))
+        *reinterpret_cast<float2*>(y) = odd ? make_float2(o, v[i + 1]) : make_float2(v[i], o);
       y += 2 * p.ldy;
     }
   } else if constexpr (OUT < 2) {
-    const bool in = n < p.N && NV_IDX(t < p.M);
+    const bool in = n < p.N;
     uint8_t* y = static_cast<uint8_t*>(p.y) + (t * p.ldy + n) * (OUT == 0 ? 4 : 2);
 #pragma unroll
     for (int i = 0; i < CNT; ++i) {
-      if (in && i < count) {
+      if (in && i < count && NV_IDX(in_matrix(t + i, n, 1, p.M, p.N, p.ldy))) {
         if (OUT == 0) *reinterpret_cast<float*>(y) = v[i];
         else *reinterpret_cast<uint16_t*>(y) = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
       }
@@ -152,12 +154,12 @@ __device__ __forceinline__ void store_lanes(const SmallParams& p, int64_t t, int
       const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w, d);
       w = (lane & d) == 0 ? (w & low) | ((o & low) << (4 * d)) : (w & ~low) | ((o & ~low) >> (4 * d));
     }
-    if (l8 < count && l8 < CNT && NV_IDX(t + l8 < p.M)) {
+    if (l8 < count && l8 < CNT) {
       const int64_t r = t + l8;
-      if (in) *reinterpret_cast<uint32_t*>(p.q_codes + r * (p.N / 2) + (n - l8) / 2) = w;
-      if (lane < 8)
-        p.q_scales[tiled_at(r, (n - lane) / 128, (p.N + 127) / 128, static_cast<int>((n - lane) / 32 % 4))] =
-            static_cast<uint8_t>(in ? sb : 0u);
+      if (in && NV_IDX(in_matrix(r, (n - l8) / 2, 4, p.M, p.N / 2, p.N / 2)))
+        *reinterpret_cast<uint32_t*>(p.q_codes + r * (p.N / 2) + (n - l8) / 2) = w;
+      const int64_t s = tiled_at(r, (n - lane) / 128, (p.N + 127) / 128, static_cast<int>((n - lane) / 32 % 4));
+      if (lane < 8 && NV_IDX(s < scale_extent(p.M, p.N, 1, 32))) p.q_scales[s] = static_cast<uint8_t>(in ? sb : 0u);
     }
   }
 }
@@ -167,7 +169,8 @@ struct Block {
   uint4 v[4];
 };
 __device__ __forceinline__ void load_block(const SmallParams& p, int row, int64_t col, Block& b) {
-  const bool in = row < p.M && col < p.K;          // K % 32 == 0: a block is in or out
+  const bool in = row < p.M && col < p.K &&        // K % 32 == 0: a block is in or out
+                  NV_IDX(in_matrix(row, col, 32, p.M, p.K, p.ldx));
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     b.v[i] = in ? ld_nc_v4(p.x + row * p.ldx + col + 8 * i) : make_uint4(0, 0, 0, 0);
@@ -370,7 +373,8 @@ mx4_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant_
     if (OUT == 2 && sidx == 0 && t0 + NT >= p.M && (p.M & 127) != 0) {
       // the scale rows behind the last token (128-row padding of this atom)
       const int64_t r = (p.M & ~127ll) + 32 * q + lane;
-      if (r >= p.M) *reinterpret_cast<uint32_t*>(p.q_scales + tiled_at(r, nt, (p.N + 127) / 128, 0)) = 0u;
+      const int64_t s = tiled_at(r, nt, (p.N + 127) / 128, 0);
+      if (r >= p.M && NV_IDX(s + 4 <= scale_extent(p.M, p.N, 1, 32))) *reinterpret_cast<uint32_t*>(p.q_scales + s) = 0u;
     }
     if (lane == 0) good = mbar_wait(done, 0, p.err) && good;
     good = __shfl_sync(0xFFFFFFFFu, good, 0);

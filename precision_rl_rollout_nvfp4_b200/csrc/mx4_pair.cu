@@ -73,7 +73,7 @@ __device__ __forceinline__ void store_rows(const PairParams& p, const uint8_t* s
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = i * 4 + (lane >> 3);
-      if (row0 + r < p.M && NV_IDX(row0 + r < p.M && col + PER <= p.N))
+      if (row0 + r < p.M && NV_IDX(in_matrix(row0 + r, col, PER, p.M, p.N, p.ldy)))
         *reinterpret_cast<uint4*>(y + ((row0 + r) * p.ldy + col) * SIZE) =
             *reinterpret_cast<const uint4*>(stg + r * Pair<OUT>::STRIDE + 16 * (lane & 7));
     }
@@ -81,7 +81,7 @@ __device__ __forceinline__ void store_rows(const PairParams& p, const uint8_t* s
 #pragma unroll 8
     for (int i = 0; i < COLS; ++i) {
       const int r = OUT == 0 ? i : i >> 1, c = OUT == 0 ? lane : (i & 1) * 32 + lane;
-      if (row0 + r < p.M && col0 + c < p.N && NV_IDX(row0 + r < p.M)) {
+      if (row0 + r < p.M && col0 + c < p.N && NV_IDX(in_matrix(row0 + r, col0 + c, 1, p.M, p.N, p.ldy))) {
         if (OUT == 0)
           reinterpret_cast<uint32_t*>(y)[(row0 + r) * p.ldy + col0 + c] =
               *reinterpret_cast<const uint32_t*>(stg + r * Pair<OUT>::STRIDE + 4 * c);
@@ -199,16 +199,16 @@ __device__ __forceinline__ void drain(const PairParams& p, uint32_t trow, uint8_
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = 16 * i + (lane >> 1);
-        if (row0 + r < p.M && col < p.N && NV_IDX(row0 + r < p.M && col + 32 <= p.N))
+        if (row0 + r < p.M && col < p.N && NV_IDX(in_matrix(row0 + r, col / 2, 16, p.M, p.N / 2, p.N / 2)))
           *reinterpret_cast<uint4*>(p.q_codes + (row0 + r) * (p.N / 2) + col / 2) =
               *reinterpret_cast<const uint4*>(stg + r * Pair<OUT>::STRIDE + 16 * (lane & 1));
       }
       // scales: this tile is one atom wide, the warp's two blocks half of a
       // row's word; the rows behind the last one up to the padding's end get zeros
       const int64_t row = row0 + lane;
-      if (row < (p.M + 127) / 128 * 128)
-        *reinterpret_cast<uint16_t*>(p.q_scales + tiled_at(row, ct, (p.N + 127) / 128, 2 * half)) =
-            static_cast<uint16_t>(row < p.M ? word : 0u);
+      const int64_t s = tiled_at(row, ct, (p.N + 127) / 128, 2 * half);
+      if (row < (p.M + 127) / 128 * 128 && NV_IDX(s + 2 <= scale_extent(p.M, p.N, 1, 32)))
+        *reinterpret_cast<uint16_t*>(p.q_scales + s) = static_cast<uint16_t>(row < p.M ? word : 0u);
       __syncwarp();
     }
   } else {
