@@ -454,12 +454,34 @@ class _FakeQuantSTE(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, g):
+        _check_backward(g, "fake_quant")
         return g, None
+
+
+class _CheckedInput(torch.autograd.Function):
+    """x itself; a captured backward pass that could not accumulate x's gradient
+    is refused before it reaches it."""
+
+    @staticmethod
+    def forward(ctx, x):
+        return x.view_as(x)
+
+    @staticmethod
+    def backward(ctx, g):
+        _check_backward(g, "qat_linear")
+        return g
+
+
+def _check_backward(g, where):
+    if g.is_cuda and torch.cuda.is_current_stream_capturing() and not isinstance(_host, _NoHost):
+        _host.backward_capturable(where)
 
 
 def fake_quant(t, fmt="nvfp4"):
     """Trainer-side fake quantization to NVFP4 or MXFP4 (fmt="mxfp4") with a
-    straight-through gradient."""
+    straight-through gradient.  A captured backward pass is refused while an
+    eager graph of the same leaf, built on the default stream, lives (MXFP4:
+    already the captured call)."""
     _format(fmt)
     if fmt == "mxfp4" and torch.is_grad_enabled():
         _host.capturable(t, "fake_quant")
@@ -473,8 +495,11 @@ def qat_linear(x, w, act_quant=False, fmt="nvfp4"):
     dX = dY W' and dW = dY^T X' through the straight-through quantizers.
     fmt: "nvfp4" or "mxfp4"."""
     wq = fake_quant(w, fmt)
-    xq = fake_quant(x, fmt) if act_quant else x
-    return xq @ wq.t()
+    if act_quant:
+        x = fake_quant(x, fmt)
+    elif x.is_cuda and x.requires_grad and torch.cuda.is_current_stream_capturing():
+        x = _CheckedInput.apply(x)
+    return x @ wq.t()
 
 
 @dataclass

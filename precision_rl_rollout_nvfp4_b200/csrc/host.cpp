@@ -13,9 +13,15 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/function.h>
+#include <torch/csrc/autograd/functions/accumulate_grad.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/graph_task.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/autograd/variable.h>
+
+#include <unordered_set>
+#include <vector>
 
 #include "nvfp4rac.h"
 
@@ -522,6 +528,56 @@ Tensor fake_quantized(const Tensor& t, int64_t fmt) {
   return out;
 }
 
+// A leaf's gradient accumulator belongs to the stream on which the first graph
+// that holds it was built.  If that is the default stream, which no capture can
+// join, a captured backward pass that reaches it ends the process.
+bool on_default_stream(torch::autograd::Node& accumulator) {
+  const auto s = accumulator.stream();
+  return s.has_value() && c10::cuda::CUDAStream(*s) == c10::cuda::getDefaultCUDAStream(s->device_index());
+}
+constexpr const char* kEagerGraph =
+    ": captured while an eager graph of the same leaf, built on the default stream, lives; "
+    "release it (its loss and outputs) before the capture";
+
+// Called by a node of this package in its backward pass: refuses a captured one
+// before the gradients it returns reach such an accumulator, directly or through
+// the nodes between (a leaf's views, other layers).  Nodes that this pass does
+// not run (torch.autograd.grad with respect to something nearer) do not count.
+void check_backward(const char* where) {
+  if (c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None) return;
+  const auto from = torch::autograd::get_current_node();
+  if (from == nullptr) return;
+  const auto* run = torch::autograd::get_current_graph_task_exec_info();
+  std::vector<torch::autograd::Node*> todo{from.get()};
+  std::unordered_set<torch::autograd::Node*> seen{from.get()};
+  while (!todo.empty()) {
+    torch::autograd::Node* n = todo.back();
+    todo.pop_back();
+    for (const auto& e : n->next_edges()) {
+      torch::autograd::Node* f = e.function.get();
+      if (f == nullptr || !seen.insert(f).second) continue;
+      if (run != nullptr && !run->empty()) {
+        const auto it = run->find(f);
+        if (it == run->end() || !it->second.should_execute()) continue;
+      }
+      if (dynamic_cast<torch::autograd::AccumulateGrad*>(f) != nullptr)
+        TORCH_CHECK(!on_default_stream(*f), where, kEagerGraph);
+      todo.push_back(f);
+    }
+  }
+}
+
+// check_backward(name of the call)
+PyObject* backward_capturable(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HOST_BEGIN
+  WANT(1)
+  const char* where = PyUnicode_AsUTF8(a[0]);
+  if (where == nullptr) return nullptr;
+  check_backward(where);
+  Py_RETURN_NONE;
+  HOST_END
+}
+
 // The gated projection as one autograd node: on fake-quantized weights with
 // fmt, and activations with act_quant; the gradient crosses the fake quantizers
 // unchanged.
@@ -547,6 +603,7 @@ struct GatedLinear : public torch::autograd::Function<GatedLinear> {
     {
       const at::NoGradGuard no_grad;
       const c10::cuda::CUDAGuard guard(s[0].device());
+      check_backward("gated_linear");
       backward_call(s[0], s[1], s[2], dh[0], static_cast<int>(ctx->saved_data["act"].toInt()), s[3], need, grad);
     }
     torch::autograd::variable_list given;
@@ -566,20 +623,15 @@ struct GatedLinear : public torch::autograd::Function<GatedLinear> {
   }
 };
 
-// Refuses a differentiable call that is being captured while an eager graph
-// of the same leaf lives.  The leaf's gradient accumulator belongs to the stream
-// on which that graph was built; if it is the default stream, which no capture
-// can join, the captured backward pass would end the process there.
+// Refuses a differentiable call on a leaf that is being captured while an eager
+// graph of that leaf, built on the default stream, lives: before anything of it
+// is captured, where check_backward would refuse its backward pass.
 void check_capture(std::initializer_list<const Tensor*> leaves, const char* where) {
   if (c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None) return;
   for (const Tensor* t : leaves) {
     if (!t->requires_grad() || !t->is_leaf()) continue;
     const auto node = torch::autograd::impl::try_get_grad_accumulator(*t);
-    if (node == nullptr) continue;
-    const auto s = node->stream();
-    TORCH_CHECK(!s.has_value() || c10::cuda::CUDAStream(*s) != c10::cuda::getDefaultCUDAStream(s->device_index()), where,
-                ": captured while an eager graph of the same leaf, built on the default stream, lives; "
-                "release it (its loss and outputs) before the capture");
+    TORCH_CHECK(node == nullptr || !on_default_stream(*node), where, kEagerGraph);
   }
 }
 
@@ -640,7 +692,8 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(init),   METHOD(quantize), METHOD(qdq),           METHOD(dequantize),
                          METHOD(gemm),   METHOD(gated_gemm), METHOD(linear),      METHOD(mlp),
-                         METHOD(gated_forward), METHOD(gated_backward), METHOD(gated_linear), METHOD(capturable), {nullptr, nullptr, 0, nullptr}};
+                         METHOD(gated_forward), METHOD(gated_backward), METHOD(gated_linear), METHOD(capturable),
+                         METHOD(backward_capturable), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_host", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
