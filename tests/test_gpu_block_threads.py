@@ -112,3 +112,33 @@ def test_weight_gradients_beside_a_thread_that_refills_the_activations():
     for dx, dg, du in got:
         assert torch.equal(dx, refs[0][0])
         assert set(match(dg, [r[1] for r in refs])) & set(match(du, [r[2] for r in refs]))
+
+
+def test_threads_on_streams_of_their_own():
+    """Calls and backward passes from several threads at once, each on its own
+    stream; every pass of every thread is counted."""
+    b = need_gpu()
+    n, work = 20, []
+    for M in (40, 300, 1):
+        x, wg, wu, dh = rows(M, 96, M), weight(96, 96, 1, 0.3), weight(96, 96, 2, 0.3), rows(M, 96, M + 1)
+        leaves = [t.requires_grad_(True) for t in (x, wg, wu)]
+        want = torch.autograd.grad(b.gated_linear(*leaves), leaves, dh)
+        qs = [b.mxfp4_quantize(t.detach()) for t in (wg, wu, wg)]
+        work.append(([x, wg, wu, dh], want, qs, b.mxfp4_gated_mlp(x.detach(), *qs)))
+    torch.cuda.synchronize()
+    done = [0] * len(work)
+
+    def run(i):
+        (*ops, dh), want, qs, y = work[i]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(n):
+                leaves = [t.detach().clone().requires_grad_(True) for t in ops]
+                got = torch.autograd.grad(b.gated_linear(*leaves), leaves, dh)
+                z = b.mxfp4_gated_mlp(leaves[0].detach(), *qs)
+                torch.cuda.current_stream().synchronize()
+                assert all(torch.equal(p, q) for p, q in zip(got, want)) and torch.equal(z, y)
+                done[i] += 1
+
+    together(*[lambda i=i: run(i) for i in range(len(work))])
+    ok(b)
+    assert done == [n] * len(work)
