@@ -454,7 +454,8 @@ nvfp4_status mxfp4_gated_gemm(const mxfp4_tensor* qx, const mxfp4_tensor* q_gate
                               void* stream);
 
 /* mxfp4_linear -- Y = Q(X) W^T for bf16 x [M, K]: mxfp4_quantize into the
- * workspace, then mxfp4_gemm_quantized.
+ * workspace, then mxfp4_gemm_quantized (one kernel for up to 4 rows).  Y may
+ * lie over x, which is read whole before Y is written.
  * ws: nvfp4_workspace_size(NVFP4_OP_MXFP4_LINEAR, M, 0, K, 1) bytes. */
 nvfp4_status mxfp4_linear(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const mxfp4_tensor* qw, void* y,
                           int32_t y_dtype, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
@@ -462,6 +463,7 @@ nvfp4_status mxfp4_linear(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, 
 /* mxfp4_gated_mlp -- the gated feed-forward block on MXFP4 weights:
  * Y = Q(H) Wd^T, H = act(Q(X) Wg^T) * (Q(X) Wu^T), for bf16 x [M, K], q_gate
  * and q_up [F, K], q_down [N, F] (scale_layout 1, F % 32 == 0); three launches.
+ * Y may lie over x.
  * ws: nvfp4_workspace_size(NVFP4_OP_MXFP4_MLP, M, F, K, 1) bytes. */
 nvfp4_status mxfp4_gated_mlp(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const mxfp4_tensor* q_gate,
                              const mxfp4_tensor* q_up, const mxfp4_tensor* q_down, int32_t act, void* y,

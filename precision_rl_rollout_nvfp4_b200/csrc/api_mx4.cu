@@ -51,6 +51,11 @@ bool out_aligned(const void* y, int32_t y_dtype) {
   return (reinterpret_cast<uintptr_t>(y) & (y_dtype == 0 ? 3u : 1u)) == 0;
 }
 
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return p < q + static_cast<uintptr_t>(b_bytes) && q < p + static_cast<uintptr_t>(a_bytes);
+}
+
 mxfp4_tensor carve(uint8_t*& at, int64_t rows, int64_t cols) {
   mxfp4_tensor t{};
   t.codes = at;
@@ -201,7 +206,9 @@ nvfp4_status mxfp4_linear(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* at = static_cast<uint8_t*>(ws);
   const mxfp4_tensor qx = carve(at, M, K);
-  const bool fused = mx4_takes_bf16(M);
+  // (a product that quantizes X itself reads it while Y is being written)
+  const bool fused = mx4_takes_bf16(M) && !overlap(x, ((M - 1) * ldx + K) * 2, y,
+                                                   ((M - 1) * ldy + qw->rows) * (y_dtype == 0 ? 4 : 2));
   if (!fused) NV_TRY(launch_mx4_quant(x, M, K, ldx, qx.codes, qx.scales, 1, nullptr, 0, s));
   NV_TRY(product(qx, fused ? x : nullptr, ldx, *qw, nullptr, 0, y, y_dtype, ldy, nullptr, s));
   return NVFP4_OK;

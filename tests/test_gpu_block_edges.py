@@ -233,3 +233,46 @@ def test_results_repeat_bit_for_bit(M):
         del junk
         assert all(torch.equal(p, r) for p, r in zip(once(), first))
     ok(b)
+
+
+# ---- outputs over the inputs, and far offsets -----------------------------------------------
+@pytest.mark.parametrize("M", [1, 2, 4, 5, 40, 300])
+def test_output_over_the_input(M):
+    """The linear and the block read all of x before they write y."""
+    b = need_gpu()
+    K, F = 2048, 512
+    x = bf16(M, K, M).cuda()
+    qw = b.mxfp4_quantize(bf16(K, K, 1, 0.02).cuda())
+    block = [b.mxfp4_quantize(t.cuda()) for t in (bf16(F, K, 2, 0.02), bf16(F, K, 3, 0.02), bf16(K, F, 4, 0.02))]
+    ref, ref_block = b.mxfp4_linear(x, qw), b.mxfp4_gated_mlp(x, *block)
+    for _ in range(20):
+        for f, want in ((lambda t: b.mxfp4_linear(t, qw, out=t), ref), (lambda t: b.mxfp4_gated_mlp(t, *block, out=t), ref_block)):
+            y = x.clone()
+            f(y)
+            assert torch.equal(y, want)
+    # y starts inside x's rows
+    buf = torch.zeros(M, K + 64, dtype=torch.bfloat16, device="cuda")
+    buf[:, :K] = x
+    b.mxfp4_linear(buf[:, :K], qw, out=buf[:, 64:])
+    ok(b)
+    assert torch.equal(buf[:, 64:], ref)
+
+
+def test_gated_projection_beyond_32_bit_offsets():
+    """More than 2^31 outputs: the last tokens' results are those of a call of
+    their own; the tokens before them are zero and add nothing to dW."""
+    b = need_gpu()
+    K, F, n = 16, 8192, 300
+    M = 64 * 4219 + n                              # (the last tokens start on a step of the reduction)
+    x, wg, wu, dh = (t.cuda() for t in (bf16(n, K, 1), bf16(F, K, 2), bf16(F, K, 3), bf16(n, F, 4)))
+    xs, ds = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda"), torch.zeros(M, F, dtype=torch.bfloat16, device="cuda")
+    xs[-n:], ds[-n:] = x, dh
+    h, saved = b.gated_linear_forward(xs, wg, wu, save=True)
+    few, few_saved = b.gated_linear_forward(x, wg, wu, save=True)
+    assert M * F > 1 << 31 and torch.equal(h[-n:], few) and not h[:-n].any()
+    del h
+    got = b.gated_linear_backward(xs, wg, wu, ds, saved=saved)
+    want = b.gated_linear_backward(x, wg, wu, dh, saved=few_saved)
+    ok(b)
+    assert torch.equal(got[0][-n:], want[0]) and not got[0][:-n].any()
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
