@@ -454,7 +454,7 @@ nvfp4_status mxfp4_gated_gemm(const mxfp4_tensor* qx, const mxfp4_tensor* q_gate
                               void* stream);
 
 /* mxfp4_linear -- Y = Q(X) W^T for bf16 x [M, K]: mxfp4_quantize into the
- * workspace, then mxfp4_gemm_quantized (one kernel for up to 4 rows).  Y may
+ * workspace, then mxfp4_gemm_quantized (one kernel for up to 8 rows).  Y may
  * lie over x, which is read whole before Y is written.
  * ws: nvfp4_workspace_size(NVFP4_OP_MXFP4_LINEAR, M, 0, K, 1) bytes. */
 nvfp4_status mxfp4_linear(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, const mxfp4_tensor* qw, void* y,

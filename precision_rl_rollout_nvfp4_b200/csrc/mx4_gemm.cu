@@ -534,10 +534,11 @@ cudaError_t small_any(const Mx4Gemm& g, cudaStream_t s) {
 
 }  // namespace
 
-// Measured (us, 4096 -> 11008, quantizing in the product against a launch of
-// its own, which costs the host 3 us more): 6.7 / 7.6 for one token, 7.4 / 7.8
-// for 4, 8.0 / 7.8 for 8, 9.7 / 7.2 for 16.
-bool mx4_takes_bf16(int64_t M) { return M <= 4; }
+// Up to 8 tokens.  Measured (us a call, cold weights, quantizing in the product /
+// in a launch of its own): 4096 -> 11008 4 tokens 8.0 / 9.2, 8 8.7 / 8.8, 12 9.3 /
+// 8.9, 16 10.0 / 9.5; 11008 -> 4096 4 8.0 / 9.4, 8 8.7 / 9.5, 16 10.0 / 9.7; 4096
+// -> 4096 8 5.9 / 6.8, 16 6.9 / 6.9; 2048 -> 1024 8 4.3 / 6.2.
+bool mx4_takes_bf16(int64_t M) { return M <= 8; }
 
 // Up to 32 tokens; while the tiles of 64 tokens x 128 weight rows fit the SMs at
 // once, also a plain product of more, and a gated one up to 128.  Measured (us,

@@ -37,7 +37,7 @@ def lines(M, N, rows=(), cols=()):
 
 
 # ---- infinities and NaN ----------------------------------------------------------
-@pytest.mark.parametrize("M", [2, 4, 16, 40, 600])
+@pytest.mark.parametrize("M", [2, 4, 8, 9, 16, 40, 600])
 def test_nonfinite_through_the_linear(M):
     """Tokens quantized in the product, few-token tiles, CTA pairs."""
     b = need_gpu()
@@ -236,7 +236,7 @@ def test_results_repeat_bit_for_bit(M):
 
 
 # ---- outputs over the inputs, and far offsets -----------------------------------------------
-@pytest.mark.parametrize("M", [1, 2, 4, 5, 40, 300])
+@pytest.mark.parametrize("M", [1, 2, 4, 5, 8, 9, 40, 300])
 def test_output_over_the_input(M):
     """The linear and the block read all of x before they write y."""
     b = need_gpu()
@@ -276,3 +276,17 @@ def test_gated_projection_beyond_32_bit_offsets():
     ok(b)
     assert torch.equal(got[0][-n:], want[0]) and not got[0][:-n].any()
     assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+
+
+@pytest.mark.parametrize("M", range(1, 18))
+@pytest.mark.parametrize("K,N", [(32, 40), (288, 130), (2080, 300), (8224, 260)])
+def test_few_tokens_quantized_in_the_product_or_before_it(M, K, N):
+    """The linear is its parts bit for bit on both sides of the rule, from rows of
+    a wider buffer too."""
+    b = need_gpu()
+    wide = bf16(M, K + 24, M).cuda()
+    qw = b.mxfp4_quantize(bf16(N, K, 1, 0.05).cuda())
+    for x in (wide[:, :K].contiguous(), wide[:, 8:8 + K]):
+        for dt in (torch.float32, torch.bfloat16):
+            assert torch.equal(b.mxfp4_linear(x, qw, dt), b.mxfp4_gemm(b.mxfp4_quantize(x), qw, dt))
+    ok(b)
