@@ -33,10 +33,13 @@ using namespace umma;
 //   kGradW    A = dG or dU read along its rows (MN-major), B = X likewise; the
 //             reduction runs over the tokens.
 //
-// Bound by the tensor pipe (97 % active in the gradients, 91 % in the forward
-// pass that also writes 8 bytes of projections per output).  8192 x 4096 x 11008
-// in a burst: forward 917 us (1.61 PFLOP/s), with the projections kept 996, dX
-// 915, dW 935; one cuBLAS product of that size runs at 1.53 PFLOP/s.
+// Bound by the tensor pipe in a single launch (97 % active in the gradients, 91 %
+// in the forward pass that also writes 8 bytes of projections per output), by the
+// power cap in a long run.  8192 x 4096 x 11008 (us, burst / loop of 1.5 s): forward
+// 930 / 1035 (1.59 / 1.43 PFLOP/s), with the projections kept 1014 / 1140, dX 944 /
+// 1102, dW 949 / 1117; a cuBLAS product of that size 911 / 1065.  Up to 256 tokens
+// dX has few tiles of a long reduction, which nothing splits: 104 us with the slopes
+// for one token, where reading the weights takes 28.
 // ---------------------------------------------------------------------------
 enum Mode { kForward, kGradX, kGradW };
 
@@ -281,8 +284,8 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
 // dG = dH U act'(G), dU = dH act(G) from the saved fp32 projections: a warp
 // takes a 32 x 32 block, a lane one of its rows; dH and the results pass
 // through shared memory so that global memory sees 64-byte row pieces.  Bound
-// by memory, 10 bytes read and 4 written per element: 227 us for 8192 x 11008
-// (5.6 TB/s) with a block per warp and small CTAs, so that the loads of one
+// by memory, 10 bytes read and 4 written per element: 213 to 227 us for 8192 x 11008
+// (5.6 to 5.9 TB/s) with a block per warp and small CTAs, so that the loads of one
 // run under the arithmetic of others; 271 us with as many CTAs as fit, each
 // walking over blocks.
 // ---------------------------------------------------------------------------

@@ -2,7 +2,7 @@
 // allocation on the current stream, the C call, and the autograd node of the
 // gated projection.  These operators take a few microseconds on the GPU for
 // one token; marshalled in Python a call took 11 to 18 us (here 4 to 5), and a
-// training step of 777 tokens through a Python autograd node 145 us (here 77).
+// training step of 777 tokens through a Python autograd node 145 us (here 82).
 //
 // The functions of the C ABI come as addresses from the library that the
 // binding loaded (init), so that the checked build serves here too.

@@ -13,11 +13,11 @@
 // tile's MMAs start; the rest is drained under them.  (Two slots, whose copies
 // run at most two steps ahead, cost 3 %.)
 //
-// Measured in a burst: 32768 x 4096 x 4096 209 us (5.25 PFLOP/s), 8192 x 11008 x
-// 4096 129 us (5.7), gated 8192 x 4096 x 11008 278 us (5.3).  It is bound by
-// power: under load the SM clock drops to 1.5 GHz, where this is 75 % of the
-// tensor peak; over a second at the 1000 W cap the same products take 243, 150
-// and 327 us.
+// Measured (us, burst / loop of 1.5 s at the 1000 W cap): 32768 x 4096 x 4096 219 /
+// 249 (5.0 / 4.4 PFLOP/s), 8192 x 11008 x 4096 135 / 149, gated 8192 x 4096 x 11008
+// 285 / 316.  In the loop the SM clock is 1.5 to 1.6 GHz, and this 60 to 68 % of the
+// tensor peak at that clock.  Power and operand supply bound it together: in a
+// burst 5.5 PFLOP/s became 6.0 without the scale copies, 7.4 without the loads.
 //
 // Warps: 0 loads, 1 MMA issue (leader CTA), 2..9 epilogue (two per TMEM lane
 // quadrant, each half of the columns: with four warps the epilogue of a lone

@@ -24,7 +24,7 @@ for layout in (0, 1):
         T.test_quantize_matches_oracle(M, K, layout)
 for cut in ("wide", "offset", "transposed", "expanded", "3d"):
     T.test_quantize_strides(cut)
-# few tokens (quantized in the product up to 4), 16, 32 and 64 token tiles, split over K, CTA pairs
+# few tokens (quantized in the product up to 8), 16, 32 and 64 token tiles, split over K, CTA pairs
 for dt in (torch.float32, torch.bfloat16):
     for M, K, N in [(1, 32, 1), (3, 96, 7), (4, 2080, 130), (16, 288, 128), (17, 256, 33), (33, 160, 64), (100, 544, 1001),
                     (300, 1504, 1001), (2600, 352, 2600)]:
