@@ -69,15 +69,22 @@ def tiled_index(rows, cols):
     return ((r >> 7) * -(-cols // 128) + (c >> 2)) * 512 + (r & 31) * 16 + ((r & 127) >> 5) * 4 + (c & 3)
 
 
+def logistic(w):
+    """1 / (1 + e^-w) in fp64, to a few units of the last place on both sides."""
+    e = np.exp(-np.abs(w))
+    return np.where(w >= 0, 1 / (1 + e), e / (1 + e))
+
+
 def act(g, kind):
-    """(act(g), act'(g)) in fp64."""
+    """(act(g), act'(g)) in fp64.  (1 + tanh z) / 2 is the logistic function of
+    2 z, which does not cancel at negative z."""
     g = np.asarray(g, np.float64)
     if kind == "silu":
-        s = np.where(g >= 0, 1 / (1 + np.exp(-np.abs(g))), np.exp(-np.abs(g)) / (1 + np.exp(-np.abs(g))))
+        s = logistic(g)
         return g * s, s + g * s * (1 - s)
-    c = np.sqrt(2 / np.pi)
-    t = np.tanh(c * (g + 0.044715 * g ** 3))
-    return 0.5 * g * (1 + t), 0.5 * (1 + t) + 0.5 * g * (1 - t * t) * c * (1 + 3 * 0.044715 * g * g)
+    c = 2 * np.sqrt(2 / np.pi)
+    s = logistic(c * (g + 0.044715 * g ** 3))
+    return g * s, s + g * s * (1 - s) * c * (1 + 3 * 0.044715 * g * g)
 
 
 def gated(x, wg, wu, kind, dh=None):
