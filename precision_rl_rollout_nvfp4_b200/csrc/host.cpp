@@ -401,7 +401,8 @@ PyObject* mlp(PyObject*, PyObject* const* a, Py_ssize_t n) {
   nvfp4_status st;
   {
     NoGil ng;
-    st = api.mlp(r.p(), r.M, r.K, r.ld, &g.c, &u.c, &d.c, act, y.t.data_ptr(), y.code, y.ld, ws.data_ptr(), bytes, stream_of(x));
+    st = api.mlp(r.p(), r.M, r.K, r.ld, &g.c, &u.c, &d.c, act, y.t.data_ptr(), y.code, y.ld, ws.data_ptr(), bytes,
+                 stream_of(x));
   }
   check(st, where);
   return THPVariable_Wrap(y.t);

@@ -246,7 +246,8 @@ def test_output_over_the_input(M):
     block = [b.mxfp4_quantize(t.cuda()) for t in (bf16(F, K, 2, 0.02), bf16(F, K, 3, 0.02), bf16(K, F, 4, 0.02))]
     ref, ref_block = b.mxfp4_linear(x, qw), b.mxfp4_gated_mlp(x, *block)
     for _ in range(20):
-        for f, want in ((lambda t: b.mxfp4_linear(t, qw, out=t), ref), (lambda t: b.mxfp4_gated_mlp(t, *block, out=t), ref_block)):
+        for f, want in ((lambda t: b.mxfp4_linear(t, qw, out=t), ref),
+                        (lambda t: b.mxfp4_gated_mlp(t, *block, out=t), ref_block)):
             y = x.clone()
             f(y)
             assert torch.equal(y, want)
@@ -265,7 +266,7 @@ def test_gated_projection_beyond_32_bit_offsets():
     K, F, n = 16, 8192, 300
     M = 64 * 4219 + n                              # (the last tokens start on a step of the reduction)
     x, wg, wu, dh = (t.cuda() for t in (bf16(n, K, 1), bf16(F, K, 2), bf16(F, K, 3), bf16(n, F, 4)))
-    xs, ds = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda"), torch.zeros(M, F, dtype=torch.bfloat16, device="cuda")
+    xs, ds = (torch.zeros(M, c, dtype=torch.bfloat16, device="cuda") for c in (K, F))
     xs[-n:], ds[-n:] = x, dh
     h, saved = b.gated_linear_forward(xs, wg, wu, save=True)
     few, few_saved = b.gated_linear_forward(x, wg, wu, save=True)
